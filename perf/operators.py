@@ -86,9 +86,8 @@ def draw(rng):
         return dict(c, prefix=rng.choice([0, 1, 50, 1000]))
     if op == "evict":
         budget = rng.randint(1, hi)
-        c = dict(c, kind=rng.choice(["rows", "pages", "kv4"]), budget=budget, recent=rng.randint(0, budget),
-                 shuffled=rng.random() < 0.5)
-        return dict(c, page=0) if c["kind"] == "rows" else c      # contiguous rows have no pages
+        return dict(c, kind=rng.choice(["rows", "pages", "kv4"]), budget=budget, recent=rng.randint(0, budget),
+                    shuffled=rng.random() < 0.5)
     c = dict(c, H=Hkv * rng.choice([h for h in (1, 2, 3, 4, 5, 8, 16) if h * Hkv <= 64]), append=rng.random() < 0.5,
              pairing=rng.choice(["adjacent", "half"]))
     if op == "kv4":
