@@ -484,6 +484,16 @@ constexpr uint32_t kCodeBase0 = 0x48004800u, kCodeBase1 = 0x38003800u;   // 8.0,
 constexpr uint32_t kCodeOff0 = 0xc808c808u, kCodeOff1 = 0xb880b880u;     // -8.0625, -0.5625
 constexpr float kCodeUnit = 128.0f;
 
+// Softmax weights to fp16.  P = 2^(logit - m) with m moved up as soon as a logit exceeds it by more than kMaxAhead: P is at
+// most 2^kMaxAhead, and 2^(15 - kMaxAhead) P at most 2^15.  As two fp16 numbers that product keeps 22 bits, or, where the
+// second would be subnormal, all down to its step 2^-24: a weight is off by at most 2^-22 of itself or 2^-38 of the
+// largest, whichever is more, so rows that weigh next to nothing still count by the thousand.  (Without the factor the step is
+// 2^-24, and 8192 rows of 2^-25 beside one of 1 leave the output though l sums them.)  A smaller kMaxAhead would move m, and
+// scale O, more often: normal logits of deviation 1 do so in 2 or 3 of a warp's 256 units at 2, in 17 at 0.  64 sequences
+// of 1K to 32K rows take 231 us with the factor, 228 without.
+constexpr float kMaxAhead = 2.0f;
+constexpr float kWeightUnit = 8192.0f;   // 2^(15 - kMaxAhead)
+
 struct Kv4Scale2 {
     uint32_t s, o0, o1;
 };
@@ -587,11 +597,10 @@ constexpr int kv4_teams(int HG) { return HG == 4 ? Kv4Shape<4>::kTeams : HG == 8
 // O^T = V^T P^T over 16 elements, and the query heads as the 8 columns: a decode step has 1 to 16 query heads a KV head,
 // so a tcgen05 tile of 128 rows of them would be at least 7/8 empty, and one of 128 cache rows would want fp16
 // values in shared memory first (four times the bytes that were loaded).  q and P are split into two fp16
-// numbers, 22 bits, so the result is fp32's: up to 4 heads the two parts are neighbouring columns of one
-// product, else a second product.  m moves only when a logit exceeds it by more than 8 (P stays below 2^8: fp16
-// holds that); l and O are fp32.
+// numbers, 22 bits: up to 4 heads the two parts are neighbouring columns of one
+// product, else a second product.  m moves only when a logit exceeds it by more than kMaxAhead; l and O are fp32.
 // Bound by issue slots (65% used; codes to fp16 are most of it) with the memory close behind: 64 sequences of 1K to 32K
-// rows, 32/8 heads, take 228 us, 5.0 TB/s; without the copies 212, without the products 183.
+// rows, 32/8 heads, take 231 us, 5.0 TB/s; without the copies 212, without the products 183.
 // An append form (p.k_new): the warp that has the sequence's last record evaluates the new row while the records are
 // on their way, and puts it into the cache and into its own copy of the record.
 template <int HG, bool SCORES>
@@ -896,7 +905,7 @@ __global__ void __launch_bounds__(128 * Kv4Shape<HG>::kTeams, 1) kv4_decode_kern
                     for (int e = 0; e < 4; ++e) unit[lane / kRecRows * kRec + kRecVs + 16 * e + lane % kRecRows] = 0;
                 __syncwarp();
             }
-            // ---- logits: lane (g, t) gets rows g and g + 8 of each record, of columns 2 t, 2 t + 1
+            // ---- logits (without their factor f > 0): lane (g, t) gets rows g and g + 8 of each record, of columns 2 t, 2 t + 1
             float lg[kLH][2 * kR];
 #pragma unroll
             for (int h = 0; h < kR; ++h) {
@@ -941,10 +950,6 @@ __global__ void __launch_bounds__(128 * Kv4Shape<HG>::kTeams, 1) kv4_decode_kern
                     }
                 }
             }
-#pragma unroll
-            for (int x = 0; x < kLH; ++x)
-#pragma unroll
-                for (int r = 0; r < 2 * kR; ++r) lg[x][r] *= f[x];
             if (i == special) {
 #pragma unroll
                 for (int x = 0; x < kLH; ++x)
@@ -959,7 +964,7 @@ __global__ void __launch_bounds__(128 * Kv4Shape<HG>::kTeams, 1) kv4_decode_kern
                         float *dst = p.scores + (static_cast<size_t>(b) * p.H + kvh * p.hpg + jbase + head(x)) * p.score_stride + row0 + g;
 #pragma unroll
                         for (int r = 0; r < 2 * kR; ++r)
-                            if (row0 + g + 8 * r < rows_end) dst[8 * r] = lg[x][r];
+                            if (row0 + g + 8 * r < rows_end) dst[8 * r] = lg[x][r] * f[x];
                     }
             }
             // ---- running maximum and sum
@@ -970,7 +975,8 @@ __global__ void __launch_bounds__(128 * Kv4Shape<HG>::kTeams, 1) kv4_decode_kern
                 top[x] = fmaxf(lg[x][0], lg[x][1]);
 #pragma unroll
                 for (int r = 2; r < 2 * kR; ++r) top[x] = fmaxf(top[x], lg[x][r]);
-                move |= top[x] > m[x] + 8.0f;
+                top[x] *= f[x];
+                move |= top[x] > m[x] + kMaxAhead;
             }
             if (__any_sync(0xffffffffu, move)) {
                 float r[kLH];
@@ -996,7 +1002,7 @@ __global__ void __launch_bounds__(128 * Kv4Shape<HG>::kTeams, 1) kv4_decode_kern
                 float sum = 0.f;
 #pragma unroll
                 for (int r = 0; r < 2 * kR; ++r) {
-                    lg[x][r] = ex2_approx(lg[x][r] - m[x]);
+                    lg[x][r] = ex2_approx(fmaf(lg[x][r], f[x], -m[x]));
                     sum += lg[x][r];
                 }
                 l[x] += sum;
@@ -1008,7 +1014,7 @@ __global__ void __launch_bounds__(128 * Kv4Shape<HG>::kTeams, 1) kv4_decode_kern
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     if constexpr (kPair) {
-                        const float pr = lg[0][2 * h + e], rest = pr - __half2float(__float2half_rn(pr));
+                        const float pr = lg[0][2 * h + e] * kWeightUnit, rest = pr - __half2float(__float2half_rn(pr));
                         uint32_t both;
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(both) : "f"(rest), "f"(pr));
                         pb[0][0][e] = transpose8x8(both);
@@ -1016,7 +1022,7 @@ __global__ void __launch_bounds__(128 * Kv4Shape<HG>::kTeams, 1) kv4_decode_kern
 #pragma unroll
                         for (int nt = 0; nt < kNT; ++nt) {
                             uint32_t hi, lo;
-                            h2_split(lg[2 * nt][2 * h + e], lg[2 * nt + 1][2 * h + e], hi, lo);
+                            h2_split(lg[2 * nt][2 * h + e] * kWeightUnit, lg[2 * nt + 1][2 * h + e] * kWeightUnit, hi, lo);
                             pb[nt][0][e] = transpose8x8(hi);
                             pb[nt][kTerms - 1][e] = transpose8x8(lo);
                         }
@@ -1098,7 +1104,7 @@ __global__ void __launch_bounds__(128 * Kv4Shape<HG>::kTeams, 1) kv4_decode_kern
                 O = fmaf(r, reinterpret_cast<const float *>(s_rings + w * Shape::kRing)[j * kKv4HeadPitch + tid], O);
                 L = fmaf(r, s_l[w][j], L);
             }
-            O *= kCodeUnit;
+            O *= kCodeUnit / kWeightUnit;
             if (poison) {
                 O = L = __int_as_float(0x7fc00000);
                 M = 0.f;

@@ -551,9 +551,9 @@ gqa_status gqa_kv4_read(const void *kv_pages, const int32_t *page_table, int num
 /*
  * Decode over a 4-bit cache: gqa_attn_decode_paged and gqa_attn_decode_append_paged with the
  * cached rows held as above.  The append form quantises k-hat (RMSNorm and RoPE evaluated in 64 bits,
- * rounded to bf16) and v into row seqlens[b] and attends to rows 0 .. seqlens[b].  q and the softmax
- * weights keep 22 bits and more through the matrix products: apart from the cache's own rounding the
- * result is as exact as the bf16 decode's.
+ * rounded to bf16) and v into row seqlens[b] and attends to rows 0 .. seqlens[b].  In the matrix
+ * products an element of q-hat is off by at most 2^-22 of itself or 2^-39 of its head's largest, a softmax weight
+ * by at most 2^-22 of itself or 2^-38 of the largest, so many rows of next to no weight still add up.
  *   acc        accumulated weights as for gqa_attn_decode_weights, or NULL
  *   workspace  >= gqa_attn_decode_kv4_workspace_size(B, H, Hkv, D, max_len, acc != NULL) bytes,
  *              256-byte aligned
