@@ -796,6 +796,8 @@ def _check_rows(t, name, rows, Hkv):
         return Hkv * D
     if rows and (t.stride(2) != 1 or (Hkv > 1 and t.stride(1) != D)):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
+    if rows > 1 and t.stride(0) < Hkv * D:   # an expanded tensor has 0, which the library takes for Hkv * D
+        raise ValueError(f"{name}: rows must not overlap")
     return t.stride(0) if rows > 1 else Hkv * D
 
 
@@ -833,13 +835,13 @@ def kv4_read(pages, page_table, cu_seqlens, prefix_len, N: int, k_out: Optional[
     if cu_seqlens.shape != (B + 1,):
         raise ValueError("cu_seqlens must be [B+1] and prefix_len [B]")
     num_pages, page_size, max_pages, Hkv = _check_kv4(pages, page_table, B)
+    ks, vs = (Hkv * D if t is None else _check_rows(t, name, N, Hkv) for t, name in ((k_out, "k_out"), (v_out, "v_out")))
+    if any(t is not None and t.shape[2] != D for t in (k_out, v_out)):
+        raise ValueError(f"k_out and v_out must be [N, Hkv, {D}]")
 
     def call(st):
         k = k_out if k_out is not None else pages.new_empty((N, Hkv, D), dtype=torch.bfloat16)
         v = v_out if v_out is not None else pages.new_empty((N, Hkv, D), dtype=torch.bfloat16)
-        ks, vs = _check_rows(k, "k_out", N, Hkv), _check_rows(v, "v_out", N, Hkv)
-        if k.shape[2] != D or v.shape[2] != D:
-            raise ValueError(f"k_out and v_out must be [N, Hkv, {D}]")
         _raise(lib.gqa_kv4_read(_ptr(pages), _ptr(page_table), num_pages, page_size, max_pages, _ptr(cu_seqlens),
                                 _ptr(prefix_len), _ptr(k), ks, _ptr(v), vs, B, N, Hkv, D, st), "gqa_kv4_read")
         return k, v
