@@ -539,6 +539,14 @@ def attn_block_prefill(x, w_qkv, w_o, pos, qnorm_w, knorm_w, H: int, Hkv: int, e
     return out
 
 
+def _check_step(B: int, D: int, seqlens, q_pos, *norms):
+    """What a decode step reads an entry of for every sequence or element: at least that many."""
+    if seqlens.shape[0] < B or (q_pos is not None and q_pos.shape[0] < B):
+        raise ValueError("seqlens and q_pos must be [B]")
+    if any(w.shape[0] < D for w in norms):
+        raise ValueError("qnorm_w and knorm_w must be [D]")
+
+
 def decode(q, k_cache, v_cache, cache_offsets, seqlens, qnorm_w, max_len: int,
            q_pos: Optional[torch.Tensor] = None, theta: float = 1.0e6, eps: float = 1e-6,
            out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
@@ -564,6 +572,7 @@ def decode(q, k_cache, v_cache, cache_offsets, seqlens, qnorm_w, max_len: int,
         raise ValueError("cache shape mismatch")
     if cache_offsets.shape != (B + 1,) or seqlens.shape != (B,):
         raise ValueError("cache_offsets must be [B+1] and seqlens [B]")
+    _check_step(B, D, seqlens, q_pos, qnorm_w)
     if weights is not None:
         acc = _kv_weights(weights, None, B, Hkv, max_len)
         rope = rope if rope is not None else RopeConfig.make(theta=theta)
@@ -623,6 +632,7 @@ def decode_append(q, k_new, v_new, k_cache, v_cache, cache_offsets, seqlens, qno
         raise ValueError("k_new and v_new must be [B, Hkv, D]")
     if cache_offsets.shape != (B + 1,) or seqlens.shape != (B,):
         raise ValueError("cache_offsets must be [B+1] and seqlens [B]")
+    _check_step(B, D, seqlens, q_pos, qnorm_w, knorm_w)
     if weights is not None or row_pos is not None:
         acc = _kv_weights(weights, row_pos, B, Hkv, max_len)
         rope = rope if rope is not None else RopeConfig.make(theta=theta)
@@ -679,6 +689,9 @@ def decode_paged(q, k_pages, v_pages, page_table, seqlens, qnorm_w, max_len: int
         _check(q_pos, "q_pos", torch.int32, 1)
     B, H, D = q.shape
     num_pages, page_size, Hkv, _ = _check_pages(k_pages, v_pages, page_table, B)
+    if k_pages.shape[3] != D:
+        raise ValueError("q and the pages must have one D")
+    _check_step(B, D, seqlens, q_pos, qnorm_w)
     rope = rope if rope is not None else RopeConfig.make()
     if weights is not None:
         acc = _kv_weights(weights, None, B, Hkv, max_len)
@@ -726,6 +739,9 @@ def decode_append_paged(q, k_new, v_new, k_pages, v_pages, page_table, seqlens, 
         _check(q_pos, "q_pos", torch.int32, 1)
     B, H, D = q.shape
     num_pages, page_size, Hkv, _ = _check_pages(k_pages, v_pages, page_table, B)
+    if k_pages.shape[3] != D:
+        raise ValueError("q and the pages must have one D")
+    _check_step(B, D, seqlens, q_pos, qnorm_w, knorm_w)
     if k_new.shape != (B, Hkv, D) or v_new.shape != (B, Hkv, D):
         raise ValueError("k_new and v_new must be [B, Hkv, D]")
     rope = rope if rope is not None else RopeConfig.make()
