@@ -490,7 +490,7 @@ constexpr float kCodeUnit = 128.0f;
 // largest, whichever is more, so rows that weigh next to nothing still count by the thousand.  (Without the factor the step is
 // 2^-24, and 8192 rows of 2^-25 beside one of 1 leave the output though l sums them.)  A smaller kMaxAhead would move m, and
 // scale O, more often: normal logits of deviation 1 do so in 2 or 3 of a warp's 256 units at 2, in 17 at 0.  64 sequences
-// of 1K to 32K rows take 231 us with the factor, 228 without.
+// of 1K to 32K rows take 230 us with the factor, 228 without.
 constexpr float kMaxAhead = 2.0f;
 constexpr float kWeightUnit = 8192.0f;   // 2^(15 - kMaxAhead)
 
@@ -600,7 +600,7 @@ constexpr int kv4_teams(int HG) { return HG == 4 ? Kv4Shape<4>::kTeams : HG == 8
 // numbers, 22 bits: up to 4 heads the two parts are neighbouring columns of one
 // product, else a second product.  m moves only when a logit exceeds it by more than kMaxAhead; l and O are fp32.
 // Bound by issue slots (65% used; codes to fp16 are most of it) with the memory close behind: 64 sequences of 1K to 32K
-// rows, 32/8 heads, take 231 us, 5.0 TB/s; without the copies 212, without the products 183.
+// rows, 32/8 heads, take 230 us, 5.0 TB/s; without the copies 212, without the products 183.
 // An append form (p.k_new): the warp that has the sequence's last record evaluates the new row while the records are
 // on their way, and puts it into the cache and into its own copy of the record.
 template <int HG, bool SCORES>
@@ -846,15 +846,19 @@ __global__ void __launch_bounds__(128 * Kv4Shape<HG>::kTeams, 1) kv4_decode_kern
         }
 
         // The matrix instruction cuts off what does not fit into its fp32 sums (it does not round), so a long sum of
-        // like terms would come out small: every kBatch units O is added to sums in shared memory, as of maximum m_sums.
+        // like terms would come out small: every kBatch units O is added to sums in shared memory, as of maximum m_sums, and l
+        // to l_sums (as one long sum l would round off small weights beside a large one that O holds).
         float4 *const sums = reinterpret_cast<float4 *>(s_all_rings + kTeams * 4 * Shape::kRing) +
                              (team * 4 + warp) * (Shape::kSums / 4) + lane;
-        float m_sums[kLH];
+        float m_sums[kLH], l_sums[kLH];
         auto collect = [&](bool any) {   // o += the sums so far
             if (!any) return;
             float r[kLH];
 #pragma unroll
-            for (int x = 0; x < kLH; ++x) r[x] = ex2_approx(m_sums[x] - m[x]);
+            for (int x = 0; x < kLH; ++x) {
+                r[x] = ex2_approx(m_sums[x] - m[x]);
+                l[x] = fmaf(l_sums[x], r[x], l[x]);
+            }
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
@@ -881,7 +885,11 @@ __global__ void __launch_bounds__(128 * Kv4Shape<HG>::kTeams, 1) kv4_decode_kern
                             for (int e = 0; e < 4; ++e) o[nt][n][e] = 0.f;
                         }
 #pragma unroll
-                    for (int x = 0; x < kLH; ++x) m_sums[x] = m[x];
+                    for (int x = 0; x < kLH; ++x) {
+                        m_sums[x] = m[x];
+                        l_sums[x] = l[x];
+                        l[x] = 0.f;
+                    }
                 }
             }
             if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * st, parity, p.err))) {

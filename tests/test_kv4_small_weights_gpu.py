@@ -30,10 +30,14 @@ def _dominated(gqa, hpg, n, k_scale, v_first):
     pages = torch.full((2, Hkv, page // 16, ref.RECORD), 0xee, dtype=torch.uint8)      # c = 6
     pages[..., :1024] = 0x88                                                           # c = 0
     pages[..., 2048:] = 12 * 8 + 5                                                     # 1.625 2^-3
+    like = pages[0, :, 0].clone()
     for h in range(Hkv):
-        k, v = ref.put_row(pages, 0, h, 0, torch.full((128,), 7 * k_scale).to(torch.bfloat16),
-                           torch.full((128,), v_first).to(torch.bfloat16))
-        assert (k == 7 * k_scale).all() and (v == v_first).all()
+        ref.put_row(pages, 0, h, 0, torch.full((128,), 7 * k_scale).to(torch.bfloat16), torch.zeros(128).to(torch.bfloat16))
+    if v_first == VALUE:
+        for at in (slice(1024, 2048), slice(2112, 2176)):
+            pages[0, :, 0, at] = like[:, at]
+    k, v = ref.unpack(pages[0, :, 0])
+    assert (k[:, 0] == 7 * k_scale).all() and (v[:, 0] == v_first).all() and (k[:, 1:] == 0).all() and (v[:, 1:] == VALUE).all()
     tab = torch.ones((B, n // page), dtype=torch.int32)
     tab[:, 0] = 0
     q = torch.ones((B, hpg * Hkv, 128), dtype=torch.bfloat16)
@@ -57,3 +61,15 @@ def test_weights_far_below_the_largest(gqa, hpg, k_scale):
     # weight below 2^-16 of the largest is rounded to a multiple of 2^-37 of it
     e = 2.0 ** -19 * x + 2.0 ** -17
     assert (out - want).abs().max() <= 2 * e * want + n * 2.0 ** -38 * VALUE
+
+
+@pytest.mark.parametrize("hpg", [1, 5, 16])
+@pytest.mark.parametrize("k_scale", [1.75 / 8, 1.875 / 8])
+def test_sum_of_weights_far_below_the_largest(gqa, hpg, k_scale):
+    """The same V in all rows: the output is V, if the sum of the weights holds the small ones as the products do."""
+    n = 131072
+    out = _dominated(gqa, hpg, n, k_scale, VALUE)
+    # A warp has 32768 rows, 512 of them in an accumulator (up to 64 products, each cut off by at most 2^-23 of it) and in
+    # a sum of l (up to 32 additions), then 64 such sums, then 12 of lanes and warps, l and O apart: 2^-24 each; 2^-22 for
+    # P's two parts, the rescaling by 2^x and the quotient each
+    assert (out / VALUE - 1).abs().max() <= 64 * 2.0 ** -23 + (32 + 2 * 64 + 2 * 12) * 2.0 ** -24 + 3 * 2.0 ** -22
