@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(128, (HG <= 4 ? 4 : 1)) decode_split_kernel(co
     cur_off = off0;
     load_batch(vbase, kw0, vn);
     __syncwarp();
-    if constexpr (SCORES) {   // the logits, for the weights each row receives (kv_acc_kernel)
+    if constexpr (SCORES) {   // the logits, for the weights each row receives (decode_finish_kernel)
         for (int jj = 0; jj < HG && jbase + jj < p.hpg; ++jj) {
             float *dst = p.scores + (static_cast<size_t>(b) * p.H + g * p.hpg + jbase + jj) * p.score_stride + kw0;
             for (int e = lane; e < nrow; e += 32) dst[e] = sw[e * HG + jj];

@@ -1526,7 +1526,8 @@ size_t evict_moves_bytes(int B, int Hkv, int max_len, int budget) {
 
 // Threads of a selecting CTA: as many as leave all pairs resident at a time (registers for 1024 threads an SM), or as its
 // shared memory leaves to it, but at least two rows a thread.  On 512 pairs of 2080 rows 256 threads take 24 us, 512
-// 29 us; on 128 of up to 8192 rows 1024 take 34 us, 512 43 us.
+// 29 us; on 128 of up to 8192 rows 1024 take 34 us, 512 43 us.  `rows` is the caller's bound: the 2080 rows take 61 us with
+// one of 4096 and 86 us with one of 32768.
 unsigned select_threads(unsigned pairs, int rows, size_t smem) {
     const size_t resident = (227u << 10) / (smem + (26u << 10));   // CTAs an SM has shared memory for
     unsigned t = pairs <= 148 || resident < 2 ? 1024 : pairs <= 296 || resident < 4 ? 512 : 256;

@@ -599,8 +599,9 @@ constexpr int kv4_teams(int HG) { return HG == 4 ? Kv4Shape<4>::kTeams : HG == 8
 // values in shared memory first (four times the bytes that were loaded).  q and P are split into two fp16
 // numbers, 22 bits: up to 4 heads the two parts are neighbouring columns of one
 // product, else a second product.  m moves only when a logit exceeds it by more than kMaxAhead; l and O are fp32.
-// Bound by issue slots (65% used; codes to fp16 are most of it) with the memory close behind: 64 sequences of 1K to 32K
-// rows, 32/8 heads, take 230 us, 5.0 TB/s; without the copies 212, without the products 183.
+// Bound by the latencies of what turns codes into fp16, which 16 warps an SM do not fill (65% of the issue slots used,
+// 1.4 of 4 warps a scheduler ready), with the memory close behind: 64 sequences of 1K to 32K rows, 32/8 heads, take 230 us, 5.0
+// TB/s; without the copies 212, without the products 182 (271 in a run long enough for the power cap to lower the clock).
 // An append form (p.k_new): the warp that has the sequence's last record evaluates the new row while the records are
 // on their way, and puts it into the cache and into its own copy of the record.
 template <int HG, bool SCORES>

@@ -4,8 +4,8 @@
 //  decode_finish_kernel: joins the chunks of a decode step, and weights[b][g][r] += sum over the query heads of
 //                     group g of 2^(S[r] - M) / L, from the logits S that the decode kernels leave in the
 //                     workspace and the joined M and L of every head.
-//  kv_select_kernel:  which rows stay (one CTA per sequence and KV head): the `budget` rows of the greatest key,
-//                     ties to the lowest row, by a radix selection over the 32-bit keys.
+//  kv_select_kernel:  which rows stay (one CTA per sequence and KV head, or a cluster of up to 8 that share the rows): the
+//                     `budget` rows of the greatest key, ties to the lowest row, by a radix selection over 32-bit keys.
 //  kv_move_kernel:    the rows themselves.  Keys are rotated before they are cached, so a sequence's rows have no
 //                     order that attention would see: kept rows below the budget stay where they are, and the i-th kept
 //                     row behind it goes to the i-th free row below it.  Sources lie behind the budget and targets
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(1024) kv_select_kernel(const __grid_constant__
 }
 
 // The listed rows of all (sequence, KV head) pairs, 8 warps a CTA.  Bound by memory: a row is read and written once
-// (bf16: 110 MB in 16 us; in 4 bits a row is 14 sectors of 32 B for 136 B, 31 MB in 18 us).
+// (bf16: 110 MB in 16 us; in 4 bits a row is 13 sectors of 32 B for 136 B, 31 MB in 18 us).
 template <int KIND>
 __global__ void __launch_bounds__(256) kv_move_kernel(const __grid_constant__ KvEvictParams p) {
     grid_dependency_wait();

@@ -459,6 +459,7 @@ gqa_status gqa_attn_decode_append_paged(const void *q, const void *k_new, const 
  *   workspace >= gqa_attn_decode_weights_workspace_size(B, H, Hkv, D, max_len) bytes (the splits'
  *             results, and the step's logits: 4 B per query head and row of max_len)
  *
+ * No prefill form yields weights: those of a prompt's rows are what the caller puts there (zeros, say).
  * A sequence that breaks its bounds keeps its weights.  So does one whose softmax is not a number (a bad
  * page id, a NaN in q or the cache); a row that was appended all the same starts at zero.
  */
@@ -558,7 +559,8 @@ gqa_status gqa_kv4_read(const void *kv_pages, const int32_t *page_table, int num
  *   workspace  >= gqa_attn_decode_kv4_workspace_size(B, H, Hkv, D, max_len, acc != NULL) bytes,
  *              256-byte aligned
  * Bounds and page ids are checked on the device as for gqa_attn_decode_paged.  What lies in the cache
- * behind a sequence's last row is never used.
+ * behind a sequence's last row is never used.  Work is split over the whole batch: the last bits of a sequence's
+ * result depend on the lengths of the others, and are the same for the same batch.
  */
 size_t gqa_attn_decode_kv4_workspace_size(int B, int H, int Hkv, int D, int max_len, int weights);
 gqa_status gqa_attn_decode_kv4(const void *q, const void *kv_pages, const int32_t *page_table,
@@ -596,7 +598,8 @@ gqa_status gqa_attn_decode_append_kv4(const void *q, const void *k_new, const vo
  *             same buffers as acc with the same stride (in place), or others that do not overlap;
  *             row_pos is NULL exactly if acc's is
  *   new_seqlens  int32 [B], min(n, budget); must not overlap seqlens
- *   max_len   host-side bound on seqlens;  budget >= 1;  0 <= recent <= budget
+ *   max_len   host-side bound on seqlens (CTAs and shared memory follow it: one near the lengths is faster than
+ *             the cache's capacity);  budget >= 1;  0 <= recent <= budget
  *   workspace >= gqa_kv_evict_workspace_size(B, Hkv, max_len, budget) bytes, 256-byte aligned
  * A sequence that breaks its bounds (0 <= n <= max_len, its rows) or names a page out of range among its
  * n rows is left untouched, new_seqlens[b] = seqlens[b], and GQA_ERR_DEVICE_INPUT is set.  B = 0 is a no-op.
